@@ -101,7 +101,8 @@ class Decoder:
     """Layers, final norm and head over one cache per layer, with every buffer a
     step of up to ``max_tokens`` tokens needs.  A step allocates its logits (and
     the rows picked for them), and attention's workspace when it needs a larger
-    one than the steps before."""
+    one than the steps before.  Whatever a step has used stays allocated as long
+    as the decoder, so a captured step can be replayed after any other."""
 
     def __init__(self, config: DecoderConfig, layers: list[DecoderLayer], final_norm, head: Linear,
                  n_pages: int, page_tokens: int = 64, max_tokens: int = 64, n_positions: int = 4096,
@@ -130,13 +131,20 @@ class Decoder:
                    for n in {min(max_tokens, TILED_MAX_BATCH), max_tokens})
         self.workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
         self.attention_workspace = torch.empty(0, dtype=torch.uint8, device=device)
+        self._outgrown: list[torch.Tensor] = []
 
     def _attend(self, cache: KvCache, tokens: int, step: StepInputs) -> None:
         c = self.config
         need = df11_attention_workspace_bytes(cache, tokens, c.heads, step.kv_lens.shape[0],
                                               step.max_queries, step.max_kv)
-        if need > self.attention_workspace.numel():
-            self.attention_workspace = torch.empty(need, dtype=torch.uint8, device=self.q.device)
+        held = self.attention_workspace.numel()
+        if need > held:
+            # The one before is kept: a graph captured with it still writes there, and
+            # so may a step on another stream.  At least doubled, so that all of them
+            # together are at most twice the last.
+            self._outgrown.append(self.attention_workspace)
+            self.attention_workspace = torch.empty(max(need, 2 * held), dtype=torch.uint8,
+                                                   device=self.q.device)
         df11_attention(cache, self.q[:tokens], step.q_start, step.kv_lens, step.page_table,
                        self.attended[:tokens], step.max_queries, step.max_kv,
                        workspace=self.attention_workspace if need else None)
