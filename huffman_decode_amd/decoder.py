@@ -102,7 +102,14 @@ class Decoder:
     step of up to ``max_tokens`` tokens needs.  A step allocates its logits (and
     the rows picked for them), and attention's workspace when it needs a larger
     one than the steps before.  Whatever a step has used stays allocated as long
-    as the decoder, so a captured step can be replayed after any other."""
+    as the decoder, so a captured step can be replayed after any other.
+
+    ``status`` (an int32 tensor of one element that the caller reads, and may
+    clear) counts what the layers left out because an index was out of range: a
+    token whose position is not in the rotary table (``n_positions``) or whose
+    slot is not in the cache, a sequence past ``max_queries`` or ``max_kv``.
+    Their logits are NaN.  A token left out has stored no key: what its slot
+    held before is what later tokens of its sequence read."""
 
     def __init__(self, config: DecoderConfig, layers: list[DecoderLayer], final_norm, head: Linear,
                  n_pages: int, page_tokens: int = 64, max_tokens: int = 64, n_positions: int = 4096,
@@ -125,7 +132,8 @@ class Decoder:
         self.residual, self.normed = new(c.hidden, dtype=bf16), new(c.hidden, dtype=bf16)
         self.qkv_out, self.hidden_out = new(c.qkv_rows, dtype=f32), new(c.hidden, dtype=f32)
         self.gate_up_out, self.act = new(2 * c.mlp, dtype=f32), new(c.mlp, dtype=bf16)
-        self.q, self.attended = (new(c.heads, c.head_dim, dtype=bf16) for _ in range(2))
+        self._left_out = torch.empty(2, max_tokens, c.heads, c.head_dim, dtype=bf16, device=device)
+        self.q, self.attended = self._left_out
         linears = [head] + [m for l in layers for m in (l.qkv, l.o, l.gate_up, l.down)]
         need = max(m.workspace_bytes(n) for m in linears
                    for n in {min(max_tokens, TILED_MAX_BATCH), max_tokens})
@@ -158,6 +166,9 @@ class Decoder:
             raise ValueError(f"{tokens} tokens, buffers for {self.residual.shape[0]}")
         x, residual = embedded, None
         h, normed = self.residual[:tokens], self.normed[:tokens]
+        # The operators leave out the rows of an index that is out of range, the same
+        # ones in every layer: such a row stays NaN instead of an earlier step's.
+        self._left_out[:, :tokens].fill_(float("nan"))
         for layer, cache in zip(self.layers, self.caches):
             if residual is None:
                 h.copy_(embedded)

@@ -106,3 +106,61 @@ def test_a_captured_step_after_a_step_that_needs_a_larger_workspace():
         assert all(bool((t == 0x5A).all()) for t in others), f"replay {r} wrote into other tensors"
         assert torch.equal(dec.forward(x[:2], step), want)
     assert int(dec.status.item()) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tokens", [1, 40])
+@pytest.mark.parametrize("wrong", ["position", "negative position", "slot", "kv_len", "queries"])
+def test_what_an_index_out_of_range_leaves_out_is_nan(wrong, tokens):
+    """A token past the rotary table or the cache, a sequence past the stated
+    limits: its logits are NaN, not numbers made of an earlier step's queries or
+    attention rows; those of the other sequence are as ever, bit by bit."""
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    page, n_pos = 16, 128
+    words, norms = _words(3)
+    dec = from_weights(CFG, words, norms, n_pages=12, page_tokens=page, max_tokens=2 * tokens, n_positions=n_pos)
+    table = torch.arange(12, dtype=torch.int32).view(2, 6).cuda()
+    g = torch.Generator().manual_seed(4)
+
+    def i32(*v):
+        return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+    def run(x, first, positions=None, slots=None, kv=None, max_queries=tokens):
+        at = torch.arange(tokens, device="cuda")
+        pos = torch.cat([at + first, at + first]).to(torch.int32)
+        seq = torch.arange(2, device="cuda").repeat_interleave(tokens)
+        own = table[seq, (pos // page).long()] * page + pos % page
+        return dec.forward(x, StepInputs(pos if positions is None else positions(pos),
+                                         own if slots is None else slots(own), i32(0, tokens, 2 * tokens),
+                                         i32(first + tokens, first + tokens) if kv is None else kv, table,
+                                         max_queries, 80))
+
+    def last(t, value):  # the last token's entry
+        t = t.clone()
+        t[-1] = value
+        return t
+    x = [torch.randn(2 * tokens, CFG.hidden, generator=g).to(BF16).cuda() for _ in range(2)]
+    run(x[0], 0)
+    want = run(x[1], tokens).clone()
+    assert torch.isfinite(want).all() and int(dec.status.item()) == 0
+    run(x[0], 0)
+    bad = torch.zeros(2 * tokens, dtype=torch.bool)
+    bad[-1] = True
+    if wrong == "position":
+        got = run(x[1], tokens, positions=lambda p: last(p, n_pos))
+    elif wrong == "negative position":
+        got = run(x[1], tokens, positions=lambda p: last(p, -1))
+    elif wrong == "slot":
+        got = run(x[1], tokens, slots=lambda s: last(s, 12 * page))
+    elif wrong == "kv_len":
+        got, bad[tokens:] = run(x[1], tokens, kv=i32(2 * tokens, 81)), True
+    else:
+        got, bad[:] = run(x[1], tokens, max_queries=tokens - 1), True
+        if tokens == 1:  # no queries at all: nothing is launched, and nothing counted
+            dec.status.fill_(1)
+    print("[gpu]", wrong, tokens, "status", int(dec.status.item()), flush=True)
+    assert int(dec.status.item()) > 0
+    nan = torch.isnan(got).cpu()
+    assert bool(nan[bad].all()) and not bool(nan[~bad].any())
+    assert torch.equal(got.cpu()[~bad], want.cpu()[~bad])
