@@ -80,6 +80,11 @@ def _stream(stream, device: int) -> int:
     return _cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
+def _too_large(name: str, *sizes: int) -> ValueError:
+    """The C calls count in 32 bits, and ctypes would cut what does not fit."""
+    return ValueError(f"{name}: sizes must be below 2**32 and not negative, not {sizes}")
+
+
 def _device(name: str, t) -> int:
     dev = t.get_device()
     if dev < 0:
@@ -102,6 +107,8 @@ def _matrix(name: str, t, dev: int, rows: int, cols: int) -> int:
             or (stride[1] != 1 and cols > 1):
         raise ValueError(f"{name} must be a [{rows}, {cols}] tensor with contiguous rows on GPU {dev}; "
                          f"it has shape {tuple(shape)}, strides {stride}, device {t.device}")
+    if (rows | cols) >> 32:
+        raise _too_large(name, rows, cols)
     return stride[0] if rows > 1 else cols
 
 
@@ -121,6 +128,8 @@ def _heads(name: str, t, dev: int, tokens: int, heads: int, dim: int) -> tuple[i
             or t.get_device() != dev or stride[2] != 1:
         raise ValueError(f"{name} must be a [{tokens}, {heads}, {dim}] tensor with contiguous heads on "
                          f"GPU {dev}; it has shape {tuple(shape)}, strides {stride}, device {t.device}")
+    if (tokens | heads) >> 32:
+        raise _too_large(name, tokens, heads)
     head = stride[1] if heads > 1 else dim
     return (stride[0] if tokens > 1 else heads * dim), head
 
@@ -249,6 +258,8 @@ def df11_logits(logits, out, tokens=None, lens=None, prompt_lens=None, repetitio
 
 def kv_block_bytes(page_tokens: int, dim: int) -> int:
     """Bytes of one page of one key head (0 for sizes the cache does not have)."""
+    if (page_tokens | dim) >> 32:
+        return 0
     return int(_lib().df11_kv_block_bytes(page_tokens, dim))
 
 
@@ -273,6 +284,8 @@ class KvCache:
             raise ValueError("status must be an int32 tensor on the pages' device")
         self.pages, self.status, self.device = pages, status, pages.get_device()
         n_pages, kv_heads = pages.shape[:2]
+        if (n_pages | kv_heads) >> 32:
+            raise _too_large("pages", n_pages, kv_heads)
         # a single head or page may carry any stride
         head = pages.stride(1) if kv_heads > 1 else block
         page = pages.stride(0) if n_pages > 1 else head * kv_heads
@@ -313,6 +326,8 @@ def df11_rope_append(cache: KvCache, q, k, v, cos, sin, positions, slots, q_out,
     if q.dtype is not k.dtype or v.dtype is not k.dtype or q_out.dtype is not torch.bfloat16:
         raise ValueError("q, k and v must have one type and q_out be bfloat16")
     n_pos, half = cos.shape
+    if half >> 31:
+        raise _too_large("cos", 2 * half)
     cs, ss = _matrix("cos", cos, dev, n_pos, half), _matrix("sin", sin, dev, n_pos, half)
     if cos.dtype is not torch.float32 or sin.dtype is not torch.float32:
         raise ValueError("cos and sin must be float32")
@@ -344,6 +359,8 @@ def df11_kv_read(cache: KvCache, slots, k_out, v_out, stream=None) -> None:
 def df11_attention_workspace_bytes(cache: KvCache, tokens: int, heads: int, batch: int,
                                    max_queries: int, max_kv: int) -> int:
     """Workspace bytes of df11_attention for these sizes (0: none needed)."""
+    if (tokens | heads | batch | max_queries | max_kv) >> 32:
+        raise _too_large("workspace", tokens, heads, batch, max_queries, max_kv)
     return int(_lib().df11_attention_workspace_bytes(cache._ref, tokens, heads, batch, max_queries,
                                                      max_kv))
 

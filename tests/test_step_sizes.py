@@ -1,0 +1,72 @@
+"""Sizes that the C calls' 32-bit counts cannot hold are refused by the wrappers:
+ctypes would cut them (2**32 rows would be none, and the call do nothing)."""
+import pytest
+import torch
+
+import huffman_decode_amd as hd
+from huffman_decode_amd import step
+
+BF16, I32 = torch.bfloat16, torch.int32
+MANY = 1 << 32
+
+
+class NoLibrary:
+    def __getattr__(self, name):
+        raise AssertionError(f"{name} was called")
+
+
+class NoCache:
+    """What the wrappers read of a cache."""
+    device, dim, kv_heads, _ref = -1, 64, 1, None
+
+
+@pytest.fixture
+def cpu(monkeypatch):
+    """CPU tensors pass for the GPU's, and nothing is called."""
+    monkeypatch.setattr(step, "_device", lambda name, t: t.get_device())
+    monkeypatch.setattr(step, "_lib", NoLibrary)
+
+
+def _rows(*shape, dtype=torch.float32):
+    """`shape` over one row's memory."""
+    return torch.zeros(1, *shape[1:], dtype=dtype).expand(*shape)
+
+
+def _refused(fn, *args, **kw):
+    with pytest.raises(ValueError, match=r"below 2\*\*3[12]"):
+        fn(*args, **kw)
+
+
+@pytest.mark.parametrize("rows", [MANY, MANY + 3])
+def test_rows(cpu, rows):
+    x, out = _rows(rows, 8), _rows(rows, 8, dtype=BF16)
+    _refused(step.df11_add_rms_norm, x, torch.ones(8), out, 1e-5)
+    _refused(step.df11_silu_mul, x, x, out)
+    _refused(step.df11_logits, x, x)
+
+
+def test_tokens_heads_and_positions(cpu):
+    i = torch.zeros(1, dtype=I32)
+    q, o, t = torch.zeros(1, 2, 64), torch.zeros(1, 2, 64, dtype=BF16), torch.zeros(1, 32)
+    kv = torch.zeros(1, 1, 64)
+    many, many_out = _rows(MANY, 2, 64), _rows(MANY, 2, 64, dtype=BF16)
+    wide, wide_out = (torch.zeros(1, 1, 64, dtype=d).expand(1, MANY, 64) for d in (torch.float32, BF16))
+    _refused(step.df11_rope_append, NoCache, many, kv, kv, t, t, i, i, many_out)
+    _refused(step.df11_rope_append, NoCache, wide, kv, kv, t, t, i, i, wide_out)
+    _refused(step.df11_rope_append, NoCache, q, kv, kv, _rows(MANY, 32), _rows(MANY, 32), i, i, o)
+    _refused(step.df11_attention, NoCache, many_out, i, i, i[None], many_out, 1, 1)
+    _refused(step.df11_attention, NoCache, wide_out, i, i, i[None], wide_out, 1, 1)
+
+
+def test_plain_numbers(cpu):
+    for n in (MANY + 1, -1):
+        for at in range(5):
+            sizes = [1, 2, 1, 1, 5000]
+            sizes[at] = n
+            _refused(step.df11_attention_workspace_bytes, NoCache, *sizes)
+
+
+def test_block_bytes():
+    assert hd.kv_block_bytes(MANY + 16, 64) == 0 and hd.kv_block_bytes(16, MANY + 64) == 0
+    assert hd.kv_block_bytes(-(MANY - 16), 64) == 0
+    assert hd.kv_block_bytes(16, 64) == 1088
