@@ -957,7 +957,11 @@ int plan_for(uint32_t dim, uint32_t kv_heads, uint32_t tokens, uint32_t heads, u
     p->nt = rows > kRows ? 2 : 1;
     const uint32_t per = p->nt * kRows * (p->shared ? 1 : kWaves);
     p->row_blocks = (uint32_t)((rows + per - 1) / per);
-    const uint64_t units = std::max<uint64_t>(1, (uint64_t)batch * kv_heads * p->row_blocks);
+    // a launch has fewer than 2^32 threads (counted in 128 bits: the product may pass 64)
+    typedef unsigned __int128 u128;
+    const u128 all = (u128)batch * kv_heads * p->row_blocks;
+    if (all > 0x00FFFFFFull) return DF11_ERR_ARG;
+    const uint64_t units = std::max<uint64_t>(1, (uint64_t)all);
     const uint32_t least = p->shared ? kSharedChunk : kRowChunk;
     const uint64_t most = std::max<uint64_t>(1, ((uint64_t)max_kv + least - 1) / least);
     const uint64_t want = std::max<uint64_t>(
@@ -966,9 +970,9 @@ int plan_for(uint32_t dim, uint32_t kv_heads, uint32_t tokens, uint32_t heads, u
     p->chunk = (uint32_t)((max_kv + want - 1) / want);
     p->chunk = std::max(p->shared && max_kv <= kWhole ? kWhole : least, (p->chunk + unit - 1) / unit * unit);
     p->splits = (uint32_t)std::max<uint64_t>(1, ((uint64_t)max_kv + p->chunk - 1) / p->chunk);
-    p->groups = (uint64_t)batch * kv_heads * p->row_blocks * p->splits;
+    p->groups = (uint64_t)all * p->splits;
     p->workspace = p->splits > 1 ? (uint64_t)p->splits * tokens * heads * (dim + 2) * 4 : 0;
-    if (p->groups > 0x00FFFFFFull) return DF11_ERR_ARG;  // a launch has fewer than 2^32 threads
+    if (p->groups > 0x00FFFFFFull) return DF11_ERR_ARG;
     return DF11_OK;
 }
 

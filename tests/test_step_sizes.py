@@ -70,3 +70,19 @@ def test_block_bytes():
     assert hd.kv_block_bytes(MANY + 16, 64) == 0 and hd.kv_block_bytes(16, MANY + 64) == 0
     assert hd.kv_block_bytes(-(MANY - 16), 64) == 0
     assert hd.kv_block_bytes(16, 64) == 1088
+
+
+def test_attention_launches_that_64_bits_cannot_count():
+    """Sequences x key heads x row blocks past 2^64: refused, not taken for the
+    few that are left of the product."""
+    import ctypes
+    kv_heads, block = 1 << 15, 1088
+    cache = step.KvCacheDesc(0x10000, kv_heads * block, kv_heads * block, block, 1, kv_heads, 64, 16, None)
+    ref = ctypes.byref(cache)
+    lib = step._lib()
+    # 2^31 sequences, 2^15 key heads, 2^18 blocks of 128 rows
+    assert lib.df11_attention_workspace_bytes(ref, 4, kv_heads, 1 << 31, 1 << 25, 5000) == 0
+    a = 0x10000
+    args = (ref, a, kv_heads * 64, 64, 4, kv_heads, a, a, 1 << 31, a, 313, 313, 1 << 25, 5000, 0.1, 1, 0, a,
+            kv_heads * 64, 64, None, a, 1 << 60, None)
+    assert lib.df11_attention(*args) == -1
