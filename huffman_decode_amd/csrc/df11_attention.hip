@@ -1024,6 +1024,8 @@ extern "C" int df11_attention(const df11_kv_cache *cache, const uint16_t *q, uin
     if (!std::isfinite(scale) || table_stride < table_cols) return DF11_ERR_ARG;
     if (max_kv > (uint64_t)table_cols * cache->page_tokens) return DF11_ERR_ARG;
     if (q_head_stride < cache->dim || out_head_stride < cache->dim) return DF11_ERR_ARG;
+    // (queries may repeat a token's row; outputs may not)
+    if (tokens > 1 && out_stride < cache->dim) return DF11_ERR_ARG;
     if (!aligned(q, 16) || q_stride % 8 || q_head_stride % 8 || !aligned(out, 16) ||
         out_stride % 8 || out_head_stride % 8 || !aligned(q_start, 4) || !aligned(kv_lens, 4) ||
         !aligned(page_table, 4) || !aligned(lse, 4))

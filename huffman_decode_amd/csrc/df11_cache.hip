@@ -472,6 +472,7 @@ extern "C" int df11_kv_read(const df11_kv_cache *cache, const int32_t *slots, ui
     if (tokens == 0) return DF11_OK;  // the arrays may be null
     if (!slots || !k_out || !v_out || cache->kv_heads > 0x3FFFu) return DF11_ERR_ARG;
     if (k_head_stride < cache->dim || v_head_stride < cache->dim) return DF11_ERR_ARG;
+    if (tokens > 1 && (k_stride < cache->dim || v_stride < cache->dim)) return DF11_ERR_ARG;
     if (!aligned(slots, 4) || !aligned(k_out, 2) || !aligned(v_out, 2)) return DF11_ERR_ARG;
     const bool vec = aligned(k_out, 16) && aligned(v_out, 16) && k_stride % 8 == 0 &&
                      k_head_stride % 8 == 0 && v_stride % 8 == 0 && v_head_stride % 8 == 0;

@@ -486,7 +486,8 @@ int df11_rope_append(const df11_kv_cache *cache, const void *q, uint64_t q_strid
 
 /* The values that slots hold, in BF16 (exact): k_out and v_out
  * [tokens][kv_heads][dim].  A negative slot reads as zeros; one out of range
- * too, and is counted in status.  Errors: ARG, BUFSIZE (cache buffer), HIP. */
+ * too, and is counted in status.  Errors: ARG (null, sizes, alignment, a token's
+ * row that lies in another's), BUFSIZE (cache buffer), HIP. */
 int df11_kv_read(const df11_kv_cache *cache, const int32_t *slots, uint16_t *k_out,
                  uint64_t k_stride, uint64_t k_head_stride, uint16_t *v_out, uint64_t v_stride,
                  uint64_t v_head_stride, uint32_t tokens, void *hip_stream);
@@ -517,7 +518,7 @@ uint64_t df11_attention_workspace_bytes(const df11_kv_cache *cache, uint32_t tok
  * each, before the sum over tokens).  Sums are formed in a fixed order: the
  * same call gives the same result on every run.
  * Errors: ARG (null, sizes, heads not a multiple, scale not finite, max_kv above
- * table_cols * page_tokens, alignment), BUFSIZE (cache buffer, workspace), HIP. */
+ * table_cols * page_tokens, alignment, an output row that lies in another's), BUFSIZE (cache buffer, workspace), HIP. */
 int df11_attention(const df11_kv_cache *cache, const uint16_t *q, uint64_t q_stride,
                    uint64_t q_head_stride, uint32_t tokens, uint32_t heads,
                    const int32_t *q_start, const int32_t *kv_lens, uint32_t batch,

@@ -86,3 +86,15 @@ def test_attention_launches_that_64_bits_cannot_count():
     args = (ref, a, kv_heads * 64, 64, 4, kv_heads, a, a, 1 << 31, a, 313, 313, 1 << 25, 5000, 0.1, 1, 0, a,
             kv_heads * 64, 64, None, a, 1 << 60, None)
     assert lib.df11_attention(*args) == -1
+
+
+def test_outputs_that_repeat_a_row_are_refused():
+    """Two tokens' results in one place: whichever came last would be left."""
+    import ctypes
+    cache = step.KvCacheDesc(0x10000, 4 * 2 * 1088, 2 * 1088, 1088, 4, 2, 64, 16, None)
+    ref, lib, a = ctypes.byref(cache), step._lib(), 0x10000
+    for out_stride in (0, 56):
+        assert lib.df11_attention(ref, a, 256, 64, 5, 4, a, a, 2, a, 3, 3, 4, 48, 0.1, 1, 0, a, out_stride, 64,
+                                  None, None, 0, None) == -1
+    for k_stride, v_stride in ((0, 128), (128, 0), (63, 128)):
+        assert lib.df11_kv_read(ref, a, a, k_stride, 64, a, v_stride, 64, 3, None) == -1
