@@ -546,6 +546,9 @@ extern "C" int df11_add_rms_norm(const void *x, uint32_t x_type, uint64_t x_stri
     if (x_stride < width || out_stride < width ||
         (residual && (residual_stride < width || residual_out_stride < width)))
         return DF11_ERR_ARG;
+    // (updated in place, a row stays where it is)
+    if (residual && residual == residual_out && rows > 1 && residual_stride != residual_out_stride)
+        return DF11_ERR_ARG;
     if (!aligned(x, size_of(x_type)) || !aligned(weight, size_of(weight_type)) ||
         !aligned(out, size_of(out_type)) || (scales && !aligned(scales, 4)) ||
         (residual && (!aligned(residual, size_of(residual_type)) ||
@@ -607,6 +610,8 @@ extern "C" int df11_logits(const void *logits, uint32_t type, uint64_t stride, f
     if (rows == 0) return DF11_OK;  // the arrays may be null
     if (!logits || !out) return DF11_ERR_ARG;
     if (stride < vocab || out_stride < vocab) return DF11_ERR_ARG;
+    // (in place, a row stays where it is)
+    if (logits == out && (type != DF11_F32 || (rows > 1 && stride != out_stride))) return DF11_ERR_ARG;
     if (history > 0x7FFFFFFFu || (history && (!tokens || !lens || tokens_stride < history)))
         return DF11_ERR_ARG;
     if (n_bias && (!bias_ids || !bias_values || bias_stride < n_bias || n_bias > 0x7FFFFFFEu))

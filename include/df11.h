@@ -390,13 +390,15 @@ enum {
 /* Residual add and root-mean-square norm of `rows` rows of `width` elements:
  *   h = x + residual,  residual_out = h,  y = h / sqrt(mean(h^2) + eps) * weight.
  * The norm takes h before its rounding to the residual's type.  residual and
- * residual_out (both null: h = x) have one type and may be the same array.
+ * residual_out (both null: h = x) have one type and may be the same array
+ * (with the same stride).
  * weight: width elements.  out is DF11_BF16 (out = y) or DF11_E4M3: then
  * a = max(largest |y| of the row, 1e-30), out = y * (448 / a) and
  * scales[row] = a / 448, so that out * scales[row] stands for y.  x, residual
  * and weight are DF11_BF16 or DF11_F32.  out must not overlap an input.
  * Errors: ARG (null, bad type, width 0, a stride below width, eps negative or
- * NaN, misalignment, scales given without DF11_E4M3 or missing with it), HIP. */
+ * NaN, misalignment, one array under two strides, scales given without
+ * DF11_E4M3 or missing with it), HIP. */
 int df11_add_rms_norm(const void *x, uint32_t x_type, uint64_t x_stride, const void *residual,
                       void *residual_out, uint32_t residual_type, uint64_t residual_stride,
                       uint64_t residual_out_stride, const void *weight, uint32_t weight_type,
@@ -422,7 +424,8 @@ int df11_silu_mul(const void *gate, uint64_t gate_stride, const void *up, uint64
  * The row's tokens are tokens[b][0 .. lens[b]) (at most `history`); those from
  * prompt_lens[b] on (null: all) were generated.  Ids outside [0, vocab) are
  * skipped.  out may be logits itself (fp32, same stride).  Errors: ARG (null,
- * vocab 0 or above 2^31 - 1, a stride below its row, misalignment), HIP. */
+ * vocab 0 or above 2^31 - 1, a stride below its row, misalignment, one array
+ * under two strides or types), HIP. */
 int df11_logits(const void *logits, uint32_t type, uint64_t stride, float *out,
                 uint64_t out_stride, const int32_t *tokens, uint64_t tokens_stride,
                 uint32_t history, const int32_t *lens, const int32_t *prompt_lens,
@@ -518,7 +521,8 @@ uint64_t df11_attention_workspace_bytes(const df11_kv_cache *cache, uint32_t tok
  * each, before the sum over tokens).  Sums are formed in a fixed order: the
  * same call gives the same result on every run.
  * Errors: ARG (null, sizes, heads not a multiple, scale not finite, max_kv above
- * table_cols * page_tokens, alignment, an output row that lies in another's), BUFSIZE (cache buffer, workspace), HIP. */
+ * table_cols * page_tokens, alignment, an output row that lies in another's),
+ * BUFSIZE (cache buffer, workspace), HIP. */
 int df11_attention(const df11_kv_cache *cache, const uint16_t *q, uint64_t q_stride,
                    uint64_t q_head_stride, uint32_t tokens, uint32_t heads,
                    const int32_t *q_start, const int32_t *kv_lens, uint32_t batch,

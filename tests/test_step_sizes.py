@@ -98,3 +98,19 @@ def test_outputs_that_repeat_a_row_are_refused():
                                   None, None, 0, None) == -1
     for k_stride, v_stride in ((0, 128), (128, 0), (63, 128)):
         assert lib.df11_kv_read(ref, a, a, k_stride, 64, a, v_stride, 64, 3, None) == -1
+
+
+def test_updates_in_place_keep_the_rows_where_they_are():
+    """One array as input and output, under two strides or types: rows would be
+    read after others were written over them."""
+    lib, a = step._lib(), 0x10000
+
+    def norm(rows, residual, residual_out, stride, out_stride):
+        return lib.df11_add_rms_norm(a, 1, 64, residual, residual_out, 0, stride, out_stride, a, 0, 1e-5, a, 0,
+                                     64, None, rows, 64, None)
+
+    def logits(rows, kind, stride, out_stride):
+        none = [None, 0, 0] + [None] * 7 + [0, 0, None, 0]
+        return lib.df11_logits(a, kind, stride, a, out_stride, *none, rows, 100, None)
+    assert norm(3, a, a, 64, 72) == -1
+    assert logits(3, 1, 100, 104) == -1 and logits(3, 0, 100, 100) == -1 and logits(1, 0, 100, 100) == -1
