@@ -944,10 +944,17 @@ constexpr uint32_t kSharedRows = 64;
 // 109, 2048 118; 64 ragged sequences of at most 8192: 78, 90, 86, 98).
 constexpr uint64_t shared_groups(uint32_t dim) { return dim == 64 ? 768 : dim == 128 ? 512 : 256; }
 constexpr uint64_t kRowGroups = 512;
-// The fewest tokens of a chunk; up to kWhole tokens a sequence is not cut at all
-// (one call of 1031 tokens: 9.7 us whole, 11.8 with a second chunk and the
-// kernel that joins them; of 2048: 12.4 and 11.8).
-constexpr uint32_t kSharedChunk = 1024, kRowChunk = 256, kWhole = 1280;
+// The fewest tokens of a chunk.
+constexpr uint32_t kSharedChunk = 1024, kRowChunk = 256;
+// Up to this many tokens a sequence of single tokens is not cut: a second chunk
+// costs the kernel that joins them, as much as 3, 2 and 1 more steps of 256
+// tokens (whole and cut, us, 1 sequence of 32 heads on 8: 64 channels 1536 tokens
+// 8.7 and 9.7, 1792 9.4 and 9.7, 1900 10.5 and 10.2; 128 channels 1281 11.1 and
+// 11.3, 1536 10.8 and 11.3, 1700 12.3 and 11.3; 256 channels 1031 17.2 and 17.3,
+// 1281 19.3 and 17.3; 8 sequences cross at the same lengths).
+constexpr uint32_t whole_tokens(uint32_t dim) {
+    return kSharedChunk + (dim == 64 ? 3 : dim == 128 ? 2 : 1) * kTile * kWaves;
+}
 
 int plan_for(uint32_t dim, uint32_t kv_heads, uint32_t tokens, uint32_t heads, uint32_t batch,
              uint32_t max_queries, uint32_t max_kv, Plan *p) {
@@ -968,7 +975,8 @@ int plan_for(uint32_t dim, uint32_t kv_heads, uint32_t tokens, uint32_t heads, u
         1, std::min(most, (p->shared ? shared_groups(dim) : kRowGroups) / units));
     const uint32_t unit = p->shared ? kTile * kWaves : kTile;
     p->chunk = (uint32_t)((max_kv + want - 1) / want);
-    p->chunk = std::max(p->shared && max_kv <= kWhole ? kWhole : least, (p->chunk + unit - 1) / unit * unit);
+    p->chunk = std::max(p->shared && max_kv <= whole_tokens(dim) ? whole_tokens(dim) : least,
+                        (p->chunk + unit - 1) / unit * unit);
     p->splits = (uint32_t)std::max<uint64_t>(1, ((uint64_t)max_kv + p->chunk - 1) / p->chunk);
     p->groups = (uint64_t)all * p->splits;
     p->workspace = p->splits > 1 ? (uint64_t)p->splits * tokens * heads * (dim + 2) * 4 : 0;

@@ -114,3 +114,17 @@ def test_updates_in_place_keep_the_rows_where_they_are():
         return lib.df11_logits(a, kind, stride, a, out_stride, *none, rows, 100, None)
     assert norm(3, a, a, 64, 72) == -1
     assert logits(3, 1, 100, 104) == -1 and logits(3, 0, 100, 100) == -1 and logits(1, 0, 100, 100) == -1
+
+
+@pytest.mark.parametrize("dim,whole", [(64, 1792), (128, 1536), (256, 1280)])
+@pytest.mark.parametrize("batch", [1, 8])
+def test_a_sequence_is_cut_where_that_was_measured_faster(dim, whole, batch):
+    """Single tokens over up to `whole` tokens: one chunk and no workspace."""
+    import ctypes
+    block = step.kv_block_bytes(64, dim)
+    cache = step.KvCacheDesc(0x10000, 64 * 8 * block, 8 * block, block, 64, 8, dim, 64, None)
+    lib, ref = step._lib(), ctypes.byref(cache)
+    for kv in (1, 1031, 1281, whole - 1, whole):
+        if kv <= whole:
+            assert lib.df11_attention_workspace_bytes(ref, batch, 32, batch, 1, kv) == 0, kv
+    assert lib.df11_attention_workspace_bytes(ref, batch, 32, batch, 1, whole + 1) == 2 * batch * 32 * (dim + 2) * 4
