@@ -161,6 +161,16 @@ __device__ __forceinline__ void value_operands(u32x4 codes, u32x4 scales, u32x4 
     }
 }
 
+// The largest scale byte that appending writes for finite values.  Above it are
+// 255 (NaN) and, in slots that nobody wrote, 253 and 254, under which codes become
+// infinities: 0 times either is NaN, so a zero weight does not hide them.
+constexpr uint32_t kTopScale = 252;
+
+// Not 0 where one of 4 scale bytes is above kTopScale.
+__device__ __forceinline__ uint32_t above_top(uint32_t bytes) {
+    return bytes & ((bytes & 0x7F7F7F7Fu) + 0x01010101u * (255u - kTopScale)) & 0x80808080u;
+}
+
 // Values of a tile: tokens 16 kg .., channel pairs n + 16 j.
 template <int DIM>
 struct ValueTile {
@@ -175,17 +185,14 @@ struct ValueTile {
             scales[j] = *(global_ptr<const u32x4>)(s + j * page_tokens);
         }
     }
-    // Scale bytes 255 (NaN) of tokens out of the product, and the 32-channel
+    // Scale bytes above kTopScale of tokens out of the product, and the 32-channel
     // groups in which a token of `seen` (the lane's 16 as bits) has one.
     __device__ __forceinline__ bool any_nan() const {
         uint32_t any = 0;
 #pragma unroll
         for (int j = 0; j < DIM / 32; ++j)
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const uint32_t b = scales[j][w];
-                any |= b & ((b & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-            }
+            for (int w = 0; w < 4; ++w) any |= above_top(scales[j][w]);
         return any != 0;
     }
     __device__ __forceinline__ uint32_t nan_groups(uint32_t seen) const {
@@ -194,7 +201,7 @@ struct ValueTile {
         for (int j = 0; j < DIM / 32; ++j)
 #pragma unroll
             for (int t = 0; t < 16; ++t)
-                if (((scales[j][t / 4] >> (8 * (t % 4))) & 255u) == 255u && ((seen >> t) & 1u))
+                if (((scales[j][t / 4] >> (8 * (t % 4))) & 255u) > kTopScale && ((seen >> t) & 1u))
                     groups |= 1u << j;
         return groups;
     }
@@ -203,7 +210,7 @@ struct ValueTile {
         for (int j = 0; j < DIM / 32; ++j)
 #pragma unroll
             for (int t = 0; t < 16; ++t)
-                if (((scales[j][t / 4] >> (8 * (t % 4))) & 255u) == 255u)
+                if (((scales[j][t / 4] >> (8 * (t % 4))) & 255u) > kTopScale)
                     scales[j][t / 4] &= ~(255u << (8 * (t % 4)));
     }
 };
@@ -401,9 +408,9 @@ __global__ __launch_bounds__(kWave *kWaves, DIM + 64 * NT <= 256 ? 2 : 1) void d
                 }
             }
             const bool partial = t0 < all_lo || t0 + kTile > all_hi || __any(!v_ok);
-            // A hidden token's value must not count even where it is NaN (0 *
-            // NaN is not 0): such scales are taken out of the product, and rows
-            // that do see one get their NaN afterwards.
+            // A hidden token's value must not count even where it is NaN or infinite
+            // (0 times that is not 0): such scales are taken out of the product, and
+            // rows that do see one get their NaN afterwards.
             bool nans = false;
             if (partial) nans = __any(vals.any_nan());
             u32x4 pf[NT][2];
@@ -545,9 +552,9 @@ __global__ __launch_bounds__(kWave *kWaves, DIM <= 128 ? 2 : 1) void df11_attent
     constexpr int kWaveRows = NT * kRows, kBlockRows = kWaves * kWaveRows;
     constexpr int kOperands = 4 * kSteps + 4 * kGroups;  // of a tile: keys [i][step], values [j][parity][s]
     __shared__ u32x4 tile[2][kOperands][kWave];
-    // per wave: bits 0..3 the 16-token parts without a page, bit 4 a NaN value scale
+    // per wave: bits 0..3 the 16-token parts without a page, bit 4 a value scale above kTopScale
     __shared__ uint32_t flags[2][kWaves];
-    __shared__ uint16_t nans[2][kGroups][4];  // tokens of a part with a NaN scale, where bit 4 is set
+    __shared__ uint16_t nans[2][kGroups][4];  // tokens of a part with such a scale, where bit 4 is set
     // (one value per wave: what follows from it stays in scalar registers)
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int n = lane % 16, kg = lane / 16;
@@ -697,10 +704,7 @@ __global__ __launch_bounds__(kWave *kWaves, DIM <= 128 ? 2 : 1) void df11_attent
 #pragma unroll
         for (int g = 0; g < kMine; ++g)
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const uint32_t b = x.vs[g][w];
-                any |= b & ((b & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-            }
+            for (int w = 0; w < 4; ++w) any |= above_top(x.vs[g][w]);
         const bool nan = __any(any != 0);
         if (nan) {  // out of the product, and noted for the rows that see them
 #pragma unroll
@@ -708,7 +712,7 @@ __global__ __launch_bounds__(kWave *kWaves, DIM <= 128 ? 2 : 1) void df11_attent
                 uint32_t tokens = 0;
 #pragma unroll
                 for (int t = 0; t < 16; ++t)
-                    if (((x.vs[g][t / 4] >> (8 * (t % 4))) & 255u) == 255u) {
+                    if (((x.vs[g][t / 4] >> (8 * (t % 4))) & 255u) > kTopScale) {
                         x.vs[g][t / 4] &= ~(255u << (8 * (t % 4)));
                         tokens |= 1u << t;
                     }

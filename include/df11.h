@@ -439,7 +439,8 @@ int df11_logits(const void *logits, uint32_t type, uint64_t stride, float *out,
  * block (page, head) starts at pages + page * page_stride + head * head_stride
  * bytes.  A value is a 4-bit float (1 sign, 2 exponent, 1 mantissa bit: 0,
  * 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) times 2^(s - 127), with one
- * scale byte s per token and 32 channels; s = 255 stands for NaN.  A block is
+ * scale byte s per token and 32 channels; s = 255 stands for NaN, and 253 and
+ * 254 are not written (a query that sees one may get NaN).  A block is
  *   key codes    [page_tokens][dim / 2]   byte: channel 2i low, 2i + 1 high
  *   value codes  [dim / 2][page_tokens]   byte: the token's channels 2i and 2i + 1
  *   key scales   [dim / 32][page_tokens]
@@ -511,7 +512,7 @@ uint64_t df11_attention_workspace_bytes(const df11_kv_cache *cache, uint32_t tok
  *   w_t = exp(scale q . k_t) / sum,  out = sum_t w_t v_t  (BF16)
  * and lse (optional, [tokens][heads] fp32) = log of that sum.  A query that sees
  * nothing gets zeros and lse -inf.  What hidden tokens, unused slots and pages
- * hold does not matter, NaN included.  Single tokens and prompts take the same
+ * hold does not matter, whatever bytes it is.  Single tokens and prompts take the same
  * call.  max_queries and max_kv bound the sequences' lengths (they size the
  * launch): a sequence with more, with negative lengths or with queries outside
  * q gets no output and is counted in status.
