@@ -81,7 +81,8 @@ def _stream(stream, device: int) -> int:
 
 
 def _too_large(name: str, *sizes: int) -> ValueError:
-    """The C calls count in 32 bits, and ctypes would cut what does not fit."""
+    """The C calls count in 32 bits, and ctypes would cut what does not fit
+    (each call looks at all its sizes at once)."""
     return ValueError(f"{name}: sizes must be below 2**32 and not negative, not {sizes}")
 
 
@@ -107,8 +108,6 @@ def _matrix(name: str, t, dev: int, rows: int, cols: int) -> int:
             or (stride[1] != 1 and cols > 1):
         raise ValueError(f"{name} must be a [{rows}, {cols}] tensor with contiguous rows on GPU {dev}; "
                          f"it has shape {tuple(shape)}, strides {stride}, device {t.device}")
-    if (rows | cols) >> 32:
-        raise _too_large(name, rows, cols)
     return stride[0] if rows > 1 else cols
 
 
@@ -128,8 +127,6 @@ def _heads(name: str, t, dev: int, tokens: int, heads: int, dim: int) -> tuple[i
             or t.get_device() != dev or stride[2] != 1:
         raise ValueError(f"{name} must be a [{tokens}, {heads}, {dim}] tensor with contiguous heads on "
                          f"GPU {dev}; it has shape {tuple(shape)}, strides {stride}, device {t.device}")
-    if (tokens | heads) >> 32:
-        raise _too_large(name, tokens, heads)
     head = stride[1] if heads > 1 else dim
     return (stride[0] if tokens > 1 else heads * dim), head
 
@@ -173,6 +170,8 @@ def df11_add_rms_norm(x, weight, out, eps: float, residual=None, residual_out=No
                 raise ValueError("residual and residual_out must have one type")
     elif residual_out is not None:
         raise ValueError("residual_out goes with residual")
+    if (rows | width) >> 32:
+        raise _too_large("x", rows, width)
     status = _lib().df11_add_rms_norm(x.data_ptr(), xt, xs, rp, rop, rt, rs, ros, wp, wt, eps,
                                       out.data_ptr(), ot, os, sp, rows, width, _stream(stream, dev))
     if status:
@@ -190,6 +189,8 @@ def df11_silu_mul(gate, up, out, stream=None) -> None:
     os, kind = _matrix("out", out, dev, rows, width), _type_of("gate", gate)
     if up.dtype is not gate.dtype or out.dtype is not torch.bfloat16:
         raise ValueError("gate and up must have one type and out be bfloat16")
+    if (rows | width) >> 32:
+        raise _too_large("gate", rows, width)
     status = _lib().df11_silu_mul(gate.data_ptr(), gs, up.data_ptr(), us, kind, out.data_ptr(), os,
                                   rows, width, _stream(stream, dev))
     if status:
@@ -247,6 +248,8 @@ def df11_logits(logits, out, tokens=None, lens=None, prompt_lens=None, repetitio
         if mask.dtype is not i32 or mask.dim() != 2 or mask.shape[1] * 32 < vocab:
             raise ValueError(f"mask must be int32 [{rows}, at least {-(-vocab // 32)}]")
         ms, mp = _matrix("mask", mask, dev, rows, mask.shape[1]), mask.data_ptr()
+    if (rows | vocab | history | n_bias) >> 32:
+        raise _too_large("logits", rows, vocab, history, n_bias)
     status = _lib().df11_logits(logits.data_ptr(), kind, ls, out.data_ptr(), os, tp, ts, history, lp,
                                 pp, rp, fp, sp, ip, vp, bs, n_bias, mp, ms, rows, vocab,
                                 _stream(stream, dev))
@@ -318,6 +321,9 @@ def df11_rope_append(cache: KvCache, q, k, v, cos, sin, positions, slots, q_out,
         raise ValueError("q must be [tokens, heads, dim] and cos [positions, rot / 2]")
     dev, dim, kv_heads = cache.device, cache.dim, cache.kv_heads
     tokens, heads = q.shape[0], q.shape[1]
+    n_pos, half = cos.shape
+    if (tokens | heads | n_pos | 2 * half) >> 32:
+        raise _too_large("q and cos", tokens, heads, n_pos, 2 * half)
     qs, qh = _heads("q", q, dev, tokens, heads, dim)
     ks, kh = _heads("k", k, dev, tokens, kv_heads, dim)
     vs, vh = _heads("v", v, dev, tokens, kv_heads, dim)
@@ -325,9 +331,6 @@ def df11_rope_append(cache: KvCache, q, k, v, cos, sin, positions, slots, q_out,
     kind = _type_of("k", k)
     if q.dtype is not k.dtype or v.dtype is not k.dtype or q_out.dtype is not torch.bfloat16:
         raise ValueError("q, k and v must have one type and q_out be bfloat16")
-    n_pos, half = cos.shape
-    if half >> 31:
-        raise _too_large("cos", 2 * half)
     cs, ss = _matrix("cos", cos, dev, n_pos, half), _matrix("sin", sin, dev, n_pos, half)
     if cos.dtype is not torch.float32 or sin.dtype is not torch.float32:
         raise ValueError("cos and sin must be float32")
@@ -345,6 +348,8 @@ def df11_kv_read(cache: KvCache, slots, k_out, v_out, stream=None) -> None:
     """The values held at ``slots`` into k_out and v_out [tokens, kv_heads, dim]
     (bfloat16, exact)."""
     dev, tokens = cache.device, slots.shape[0]
+    if tokens >> 32:
+        raise _too_large("slots", tokens)
     sp = _vector("slots", slots, dev, tokens, torch.int32)
     ks, kh = _heads("k_out", k_out, dev, tokens, cache.kv_heads, cache.dim)
     vs, vh = _heads("v_out", v_out, dev, tokens, cache.kv_heads, cache.dim)
@@ -383,6 +388,8 @@ def df11_attention(cache: KvCache, q, q_start, kv_lens, page_table, out, max_que
     if q.dtype is not torch.bfloat16 or out.dtype is not torch.bfloat16:
         raise ValueError("q and out must be bfloat16")
     batch, cols = page_table.shape
+    if (tokens | heads | batch | cols) >> 32:
+        raise _too_large("q and page_table", tokens, heads, batch, cols)
     kp = _vector("kv_lens", kv_lens, dev, batch, torch.int32)
     sp = _vector("q_start", q_start, dev, batch + 1, torch.int32)
     ts = _matrix("page_table", page_table, dev, batch, cols)
