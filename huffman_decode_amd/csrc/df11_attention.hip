@@ -264,12 +264,13 @@ struct Sight {
 // Few rows (single tokens, their groups of heads): a workgroup's 4 waves take
 // the same NT x 16 rows and every fourth tile of the chunk, and join their sums
 // through LDS at the end.  Each byte of the cache is read once, and reading it
-// is the bound: 64 sequences of 8192 tokens, 32 heads on 8 of 128 channels
-// 101 us (5.65 TB/s, 94 % of this card's read rate), 4 of 131071 tokens with 64
-// heads 107 us with the joining kernel, 64 ragged ones (at most 8192) 76 us,
-// where the longest sets the end.
+// is the bound: 64 sequences of 8192 tokens, 32 heads on 8 of 64, 128 and 256
+// channels 56, 101 and 197 us (5.1, 5.65 and 5.8 TB/s; this card reads at 6.0), 4
+// of 131071 tokens with 64 heads 107 us with the joining kernel, 64 ragged ones
+// (at most 8192) 76 us, where the longest sets the end.
 // (Two waves per SIMD where the registers allow it, or nearly: 2 x 16 rows of
-// 128 channels spill 27 registers and are 1.2 times as fast as with one.)
+// 128 channels spill 27 registers and are 1.2 times as fast as with one.  2 x 16
+// rows of 256 channels spill 110 with one wave.)
 template <int DIM, int NT>
 __global__ __launch_bounds__(kWave *kWaves, DIM + 64 * NT <= 256 ? 2 : 1) void df11_attention_kernel(
     AttnArgs a) {
@@ -536,10 +537,13 @@ __device__ __forceinline__ void lds_barrier() {
 // each wave converts a quarter of the next tile into operands in LDS (double
 // buffered, one barrier per tile; an operand is 64 lanes x 16 bytes, written and
 // read without conflicts) while all of them work on this one.  4096 queries
-// over 8192 tokens, causal, 32 heads on 8 of 128 channels (0.41 TFLOP): 421 us,
-// 0.98 PFLOP/s (an 8192^3 library product: 1.26).  Vector instructions bind (54 % of
+// over 8192 tokens, causal, 32 heads on 8 of 128 channels (0.41 TFLOP): 424 us,
+// 0.97 PFLOP/s (an 8192^3 library product: 1.26).  Vector instructions bind (55 % of
 // the time, the matrix cores 38 %, little of it together): softmax, conversion and the reads
 // of LDS operands cost 84, 84 and 108 of 429 us where left out one by one.
+// 64 channels have half the products to the same softmax: 309 us, 0.67 PFLOP/s
+// (66 and 26 %); 256 channels have one wave per SIMD, and nothing hides the
+// conversion: 1404 us, 0.59 PFLOP/s (35 and 24 %).
 // WHOLE: pages hold at least a tile, so that a tile's addresses are a scalar base
 // and lane offsets that never change.
 template <int DIM, int NT, bool WHOLE>
@@ -939,14 +943,26 @@ struct Plan {
 };
 
 // Up to this many rows of a key head, waves split the tokens; above, the rows
-// (8 sequences of 8192 tokens, 8 key heads of 128 channels: 48 rows 47 and 51 us,
-// 64 rows 49 and 52, 96 rows 79 and 57).
+// (us with either kernel, 8 key heads; 8 sequences of 8192 tokens: 64 channels
+// 64 rows 41 and 44, 80 rows 45 and 46, 128 rows 57 and 52; 128 channels 64 rows
+// 51 and 54, 80 rows 78 and 58; 256 channels 64 rows 149 and 151, 80 rows 234 and
+// 155; 32 sequences of 4096 tokens: 32 rows 41 and 63, 62 and 76, 149 and 263.
+// One sequence alone of 128 or 256 channels is faster over its rows from 20 on:
+// 20 and 16, 43 and 26).
 constexpr uint32_t kSharedRows = 64;
 // Workgroups that are resident at once on 256 compute units: a call's tokens are
 // cut to fill them at most once.  A second, partly filled round costs more than
-// uneven lengths do (4 x 131071 tokens: 512 workgroups 105 us, 768 125, 1024
-// 109, 2048 118; 64 ragged sequences of at most 8192: 78, 90, 86, 98).
+// uneven lengths do (128 channels, 4 x 131071 tokens: 512 workgroups 105 us, 768
+// 125, 1024 109, 2048 118; 64 ragged sequences of at most 8192: 78, 90, 86, 98.
+// 24 sequences of 8192: 64 channels, 512, 768 and 1024 workgroups 37, 30 and 37;
+// 256 channels, 256, 512 and 768 workgroups 89, 103 and 95).
 constexpr uint64_t shared_groups(uint32_t dim) { return dim == 64 ? 768 : dim == 128 ? 512 : 256; }
+// The same for rows, at the number that is resident for 128 channels (2 prompts
+// of 512 queries over 8192 tokens: 256, 512 and 768 workgroups 211, 187 and 200
+// us; 1 of 128 queries 45, 44 and 52).  64 channels have 768 resident and 256
+// channels 256, but what they gain depends on the rows: 64 channels 174, 155
+// and 142, 36, 33 and 35; 256 channels 457, 527 and 538, 84, 101 and 123, but 300
+// queries of 40 heads on 8 252, 228 and 235.
 constexpr uint64_t kRowGroups = 512;
 // The fewest tokens of a chunk.
 constexpr uint32_t kSharedChunk = 1024, kRowChunk = 256;

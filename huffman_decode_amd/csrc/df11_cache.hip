@@ -150,8 +150,9 @@ __device__ __forceinline__ void rotate_each(const AppendArgs &a, global_ptr<cons
 // token per workgroup took 71 us for 8191 tokens of 32 + 8 + 8 heads).
 // What bounds it is the chain position -> cosines -> result: all heads'
 // channels are loaded first, and a workgroup has several heads (VEC).  8191
-// tokens, BF16, pages of 16: 36 us for 177 MB (33 at the copy rate) with 2
-// heads; 1, 4, 8 and 12 heads took 9, 1, 7 and 13 us more, and 39 where
+// tokens, BF16, pages of 16, three sets of inputs in turn: 53 us for 177 MB (33
+// at the copy rate) with 2 heads.  On one set, which stays in the 256 MB cache,
+// 36 us; 1, 4, 8 and 12 heads took 9, 1, 7 and 13 us more, and 39 in all where
 // neighbouring tiles went to different XCDs.
 template <typename X, bool VEC, int HEADS>
 __global__ __launch_bounds__(256) void df11_rope_append_kernel(AppendArgs a) {
@@ -292,8 +293,8 @@ struct ReadArgs {
 
 // One thread gives 8 channels of one token; a workgroup has 2048 / dim
 // neighbouring tokens of one head, whose value codes it reads 4 tokens at a
-// time where their slots follow one another.  Bound by memory's latency: 8191
-// tokens of 8 heads 14 us for 42 MB.
+// time where their slots follow one another.  Bound by memory's latency (slot,
+// then scale and codes): 8191 tokens of 8 heads 15 us for 42 MB (8 at the copy rate).
 template <bool VEC>
 __global__ __launch_bounds__(256) void df11_kv_read_kernel(ReadArgs a) {
     constexpr int kMostTokens = 32, kMostWords = 256 + kMostTokens;
@@ -364,7 +365,12 @@ __global__ __launch_bounds__(256) void df11_kv_read_kernel(ReadArgs a) {
 
 int launched() { return hipGetLastError() == hipSuccess ? DF11_OK : DF11_ERR_HIP; }
 
-// Heads of a workgroup where there are workgroups enough without that.
+// Heads of a workgroup where there are workgroups enough without that: from
+// kManyGroups (tiles of tokens x heads) on.  Appending and reading back, us with 2
+// heads and with 1: 128 channels of 48 heads, BF16, 64 tokens (192) 7.6 and 6.3,
+// 1024 (3072) 14.1 and 14.3, 1536 (4608) 16.8 and 18.2, 8191 67 and 77; fp32 19.6
+// and 18.8 for 1536, 88 and 89 for 8191.  64 channels, BF16, 4096 tokens (6144)
+// 18.9 and 20.6; 256 channels of 24 heads 2048 tokens (6144) 21.3 and 22.9.
 constexpr int kHeadsHere = 2;
 constexpr uint64_t kManyGroups = 4096;
 

@@ -9,6 +9,10 @@ products decode operand tiles and multiply them on the matrix cores
 (``df11_decode_gemm_tiled``).  A longer prompt decodes each matrix once
 (``df11_decode_tiled``) and multiplies it with torch.
 
+The weights are lossless; the cache is not: keys and values are rounded to 4
+bits and a power of two per 32 channels, so logits differ from those of the
+same BF16 weights over a BF16 cache.
+
 The layer is the common pre-norm one: root-mean-square norms, grouped query
 heads with rotary positions, silu(gate) * up.  Weights are row-major [out, in]
 BF16 words; q, k and v are stacked by rows, as are gate and up.  Pages are the

@@ -205,7 +205,7 @@ def df11_logits(logits, out, tokens=None, lens=None, prompt_lens=None, repetitio
     with lens [rows]: each row's tokens, those from prompt_lens[row] on
     generated; repetition, frequency, presence [rows] float32; bias_ids
     [rows, n] int32 and bias_values [rows, n] float32 (ids outside the
-    vocabulary are skipped); mask [rows, words] int32, bit id % 32 of word
+    vocabulary are skipped, of an id listed twice the last value counts); mask [rows, words] int32, bit id % 32 of word
     id / 32 set where the id is allowed."""
     dev = _device("logits", logits)
     if logits.dim() != 2:
