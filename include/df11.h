@@ -515,7 +515,7 @@ uint64_t df11_attention_workspace_bytes(const df11_kv_cache *cache, uint32_t tok
  * hold does not matter, whatever bytes it is.  Single tokens and prompts take the same
  * call.  max_queries and max_kv bound the sequences' lengths (they size the
  * launch): a sequence with more, with negative lengths or with queries outside
- * q gets no output and is counted in status.
+ * q gets no output and is counted in status (max_queries 0 launches nothing).
  * A page number out of range hides its tokens and is counted in status.
  * q and out: 16-byte aligned, strides multiples of 8.  Scores and sums are
  * fp32; the weights w_t are rounded to BF16 as matrix operands (relative 2^-8

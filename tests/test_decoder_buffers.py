@@ -109,7 +109,7 @@ def test_a_captured_step_after_a_step_that_needs_a_larger_workspace():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("tokens", [1, 40])
+@pytest.mark.parametrize("tokens", [1, 20, 40])
 @pytest.mark.parametrize("wrong", ["position", "negative position", "slot", "kv_len", "queries"])
 def test_what_an_index_out_of_range_leaves_out_is_nan(wrong, tokens):
     """A token past the rotary table or the cache, a sequence past the stated
